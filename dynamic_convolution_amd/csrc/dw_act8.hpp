@@ -92,15 +92,16 @@ __device__ __forceinline__ uint2 act8_codes(const float (&x)[8], int e) {
     return r;
 }
 __device__ __forceinline__ float act8_step(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
-// Eight codes' values with step 2^e: (code + 128) step - 128 step, each product exact.
+// Eight codes' values with step 2^e: (code + 128) step - 128 step, each product exact while 128 steps are at most the
+// type's largest value.  The step of 2^121 of a block that reaches 2^127 makes 2^128 of them, which no fp32 holds.
 __device__ __forceinline__ void act8_values(uint2 q, int e, float most, float (&v)[8]) {
     const float step = act8_step(e), low = -128.f * step;
     const uint32_t u[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};  // code + 128 as a byte: 0 stands for a NaN
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = fmaf(static_cast<float>((u[i / 4] >> (8 * (i & 3))) & 0xffu), step, low);
-    // hardly ever: a byte of zero in either word, or steps so large that a value may pass the type's largest
+    // hardly ever: a byte of zero in either word, or steps so large that a value, or `low`, may pass the type's largest
     const uint32_t zero = ((u[0] - 0x01010101u) & ~u[0] & 0x80808080u) | ((u[1] - 0x01010101u) & ~u[1] & 0x80808080u);
-    if (zero != 0 || 127.f * step > most) {
+    if (zero != 0 || -low > most) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const bool nan = ((u[i / 4] >> (8 * (i & 3))) & 0xffu) == 0;
