@@ -126,8 +126,13 @@ struct Call {
     template <typename T = void> const T *in(int i) const {
         return args[i] == Py_None ? nullptr : static_cast<const T *>(THPVariable_Unpack(args[i]).const_data_ptr());
     }
+    // What the call writes has a new version, as after torch's own writes in place: autograd then finds a tensor that it
+    // saved before (a state that a token was added to) changed.  Inference tensors have no versions.
     template <typename T = void> T *out(int i) const {
-        return args[i] == Py_None ? nullptr : static_cast<T *>(THPVariable_Unpack(args[i]).mutable_data_ptr());
+        if (args[i] == Py_None) return nullptr;
+        const at::Tensor &t = THPVariable_Unpack(args[i]);
+        if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+        return static_cast<T *>(t.mutable_data_ptr());
     }
     size_t bytes(int i) const { return args[i] == Py_None ? 0 : THPVariable_Unpack(args[i]).nbytes(); }
 };
