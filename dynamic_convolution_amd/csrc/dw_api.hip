@@ -523,7 +523,7 @@ const char *dw_status_str(int status) {
         case DW_EMULT: return "output channels are not a multiple of input channels";
         case DW_EDTYPE: return "unknown dtype";
         case DW_EWORKSPACE: return "workspace missing, too small or not 16-byte aligned";
-        case DW_ETOOLARGE: return "a tensor has 2^31 elements or more, or an extent exceeds 2^30";
+        case DW_ETOOLARGE: return "a tensor, a size or a launch is larger than the call serves (see its header)";
         case DW_EALIAS: return "an output overlaps an input or another output";
         case DW_EHIP: return "HIP kernel launch failed";
         case DW_EDYN: return "dynamic filter: k must be odd, 1 <= nb <= 4, dilations >= 1";

@@ -1269,10 +1269,12 @@ int64_t norm_workspace(int pass, const NormSizes &s) {
     return bwd_space(s).bytes;
 }
 
-bool norm_grid_ok(const NormSizes &s) {
-    const int64_t most = int64_t{1} << 30;
-    if (s.n > most / (64 * int64_t{s.groups})) return false;
-    if (token_form(s)) return token_grid(s, 0).gblocks <= 65535;
+// What a pass's launches hold: 2^32 - 1 threads, 65535 workgroups along the groups.  The slabs' form is taken only
+// where its launch does; the join's own launch, of at most 64 lanes a group, is of at most 1024 / 3 spans of at most
+// kSpan groups (three slabs or more, see map_grid()).
+bool norm_grid_ok(int pass, const NormSizes &s) {
+    if (token_form(s)) return token_grid(s, pass).gblocks <= 65535;
+    if (!two_pass(s, pass)) return true;
     const MapGrid m = map_grid(s);
     return m.gblocks <= 65535 && s.n * m.splits * kThreads <= UINT32_MAX;
 }

@@ -93,7 +93,8 @@ struct NormSizes {
 };
 // Bytes of workspace of the forward (pass 0) or the backward (pass 1).
 int64_t norm_workspace(int pass, const NormSizes &s);
-bool norm_grid_ok(const NormSizes &s);
+// Whether a pass's launches hold these sizes.
+bool norm_grid_ok(int pass, const NormSizes &s);
 int norm_fwd_launch(const NormSizes &s, const void *x, const void *gamma, const void *beta, void *y, float *mean,
                     float *rstd, int8_t *codes, int8_t *exps, void *ws, hipStream_t stream);
 int norm_bwd_launch(const NormSizes &s, const void *dy, const void *x, const int8_t *codes, const int8_t *exps,

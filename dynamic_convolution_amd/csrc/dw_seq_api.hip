@@ -187,7 +187,7 @@ int check_act8(const void *x, const void *codes, const void *exps, int64_t rows,
 Span codes_span(const void *codes, int64_t rows, int64_t c) { return {codes, rows * c}; }
 Span exps_span(const void *exps, int64_t rows, int64_t c) { return {exps, rows * ((c + 31) / 32)}; }
 
-int check_norm(int64_t n, int64_t l, int64_t c, int64_t groups, int act, int dtype, dw::NormSizes *s) {
+int check_norm(int pass, int64_t n, int64_t l, int64_t c, int64_t groups, int act, int dtype, dw::NormSizes *s) {
     if (!known(dtype)) return DW_EDTYPE;
     if (n < 0 || l < 1 || c < 1 || groups < 1) return DW_ESHAPE;
     for (int64_t v : {n, l, c, groups})
@@ -196,7 +196,7 @@ int check_norm(int64_t n, int64_t l, int64_t c, int64_t groups, int act, int dty
     if (act != DW_ACT_NONE && act != DW_ACT_SILU && act != DW_ACT_GELU) return DW_EGROUPS;
     if (product({n, l, c}, kMaxElems) < 0) return DW_ETOOLARGE;
     *s = {n, l, c, static_cast<int>(groups), act, dtype, 0.f};
-    return n == 0 || dw::norm_grid_ok(*s) ? DW_OK : DW_ETOOLARGE;
+    return n == 0 || dw::norm_grid_ok(pass, *s) ? DW_OK : DW_ETOOLARGE;
 }
 
 // Every output against every input and every other output.
@@ -420,7 +420,7 @@ int groupnorm_act_workspace_bytes(int pass, int64_t n, int64_t l, int64_t c, int
     if (pass != 0 && pass != 1) return DW_ESHAPE;
     if (!bytes) return DW_EPTR;
     dw::NormSizes s;
-    const int rc = check_norm(n, l, c, groups, DW_ACT_NONE, dtype, &s);
+    const int rc = check_norm(pass, n, l, c, groups, DW_ACT_NONE, dtype, &s);
     if (rc != DW_OK) return rc;
     *bytes = static_cast<size_t>(dw::norm_workspace(pass, s));
     return DW_OK;
@@ -430,7 +430,7 @@ int groupnorm_act_fwd(const void *x, const void *gamma, const void *beta, void *
                       int8_t *exps, void *workspace, size_t workspace_bytes, int64_t n, int64_t l, int64_t c,
                       int64_t groups, float eps, int act, int dtype, void *stream) {
     dw::NormSizes s;
-    int rc = check_norm(n, l, c, groups, act, dtype, &s);
+    int rc = check_norm(0, n, l, c, groups, act, dtype, &s);
     if (rc != DW_OK || n == 0) return rc;
     s.eps = eps;
     const int64_t e = elem_size(dtype), rows = n * l;
@@ -457,7 +457,7 @@ int groupnorm_act_bwd(const void *dy, const void *x, const int8_t *codes, const 
                       void *workspace, size_t workspace_bytes, int64_t n, int64_t l, int64_t c, int64_t groups, int act,
                       int dtype, void *stream) {
     dw::NormSizes s;
-    int rc = check_norm(n, l, c, groups, act, dtype, &s);
+    int rc = check_norm(1, n, l, c, groups, act, dtype, &s);
     if (rc != DW_OK || n == 0) return rc;
     const int64_t e = elem_size(dtype), rows = n * l;
     for (const void *p : {dy, gamma, beta, static_cast<const void *>(dx), static_cast<const void *>(dgamma),

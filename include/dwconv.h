@@ -60,7 +60,8 @@ enum dw_status {
     DW_EDTYPE = -4,     /* dtype is not one of enum dw_dtype */
     DW_EWORKSPACE = -5, /* workspace NULL or smaller than dwconv2d_bwd_weight_workspace_bytes */
     DW_ETOOLARGE = -6,  /* some tensor has 2^31 elements or more, or an extent
-                           (size, stride, pad, dilated kernel span) exceeds 2^30 */
+                           (size, stride, pad, dilated kernel span) exceeds 2^30;
+                           the limits of dwseq.h are named there */
     DW_EALIAS = -7,     /* an output overlaps an input or another output */
     DW_EHIP = -8,       /* a HIP launch failed (hipGetLastError after the launch) */
     DW_EDYN = -9,       /* dynamic filter: k even, nb outside [1, 4], or a dilation < 1 */

@@ -8,7 +8,8 @@
  * HIP call, nothing allocated and nothing kept after a call, arithmetic and sums in fp32 or
  * wider, 16-bit results rounded to nearest-even once.  Results do not depend on timing: no
  * atomics are used.  Tensors may have more than 2^31 elements; one size is at most 2^30, an
- * offset within a tensor at most 2^46 elements, and b h at most 2^20 (DW_ETOOLARGE past those).
+ * offset within a tensor at most 2^46 elements, and b h at most 2^20; limits of single operators stand
+ * at them (DW_ETOOLARGE past any).
  */
 #ifndef DWSEQ_H
 #define DWSEQ_H
@@ -83,7 +84,7 @@ int decayattn_step(const void *q, const void *k, const void *v, const float *log
  * may be fewer) share a step 2^e, the smallest power of two, at least 2^-126, by which the largest
  * finite magnitude rounds to at most 127; a value becomes the nearest whole number of steps, ties to
  * even.  codes (rows, c) signed bytes; exps (rows, ceil(c / 32)) signed bytes, the e of each block.
- * Code -128 stands for a value that is not finite; it comes back as a NaN.
+ * Code -128 stands for a value that is not finite; it comes back as a NaN.  There may be 2^32 - 256 blocks.
  */
 int act8_pack(const void *x, int8_t *codes, int8_t *exps, int64_t rows, int64_t c, int dtype,
               void *stream);
@@ -100,6 +101,8 @@ enum dw_act { DW_ACT_NONE = 0, DW_ACT_SILU = 1, DW_ACT_GELU = 2 /* z Phi(z), by 
  * xhat = (x - mean) / sqrt(variance + eps), y = act(xhat gamma + beta).
  * gamma, beta (c) and y (n, l, c) of x's type; mean, rstd (n, groups) float.
  * codes, exps: NULL, or where x's 8-bit checkpoint goes, as act8_pack with rows = n l.
+ * Sizes: c at most 2^24 - 256; n < 2^24, or with l = 1 and c / groups <= 512 any n.  Some shapes past these are
+ * served too, others have a launch of 2^32 threads or of more than 65535 workgroups along the groups (DW_ETOOLARGE).
  * workspace: groupnorm_act_workspace_bytes(0, ...), 256-byte aligned (NULL if that is 0).
  */
 int groupnorm_act_fwd(const void *x, const void *gamma, const void *beta, void *y, float *mean,
