@@ -1004,11 +1004,12 @@ __global__ __launch_bounds__(kThreads) void norm_map_bwd_kernel(MapArgs a, const
     }
 }
 
+constexpr int kColumnThreads = 1024;
 // Column sums of part (rows, 2, c): workgroup (i, k) takes 32 columns and the k-th `chunk` of rows.  Into
 // out (chunks, 2, c) where that is given, else into dgamma and dbeta.
 template <typename T>
-__global__ __launch_bounds__(1024) void norm_column_kernel(const float *part, float *out, T *dgamma, T *dbeta, int64_t rows,
-                                                           int64_t chunk, int c) {
+__global__ __launch_bounds__(kColumnThreads) void norm_column_kernel(const float *part, float *out, T *dgamma, T *dbeta,
+                                                                     int64_t rows, int64_t chunk, int c) {
     __shared__ float sum[32][33];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + tx, last = min(rows, (blockIdx.y + int64_t{1}) * chunk);
@@ -1150,6 +1151,8 @@ int64_t part_rows(const NormSizes &s) {
 // The two-pass form of maps.
 bool two_pass(const NormSizes &s, int pass) { return !token_form(s) && !slab_grid(s, pass).threads; }
 int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
+// Workgroups of norm_column_kernel along the 2 c columns.
+uint32_t column_blocks(int64_t c) { return static_cast<uint32_t>((2 * c + 31) / 32); }
 // Chunks of the rows of partial sums: a workgroup adds 32 rows at a time, and few columns alone would
 // leave the card empty.
 int column_chunks(int64_t rows) { return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(64, rows / 512))); }
@@ -1236,16 +1239,16 @@ int bwd(const NormSizes &s, const void *dy, const void *x, const int8_t *codes, 
                            means, static_cast<T *>(dx));
     }
     T *dg = static_cast<T *>(dgamma), *db = static_cast<T *>(dbeta);
-    const uint32_t cols = static_cast<uint32_t>((2 * s.c + 31) / 32);
+    const uint32_t cols = column_blocks(s.c);
     const int c = static_cast<int>(s.c), chunks = column_chunks(rows);
     if (chunks == 1) {
-        hipLaunchKernelGGL((norm_column_kernel<T>), dim3(cols), dim3(1024), 0, st, part, nullptr, dg, db, rows, rows, c);
+        hipLaunchKernelGGL((norm_column_kernel<T>), dim3(cols), dim3(kColumnThreads), 0, st, part, nullptr, dg, db, rows, rows, c);
         return done();
     }
     float *mid = reinterpret_cast<float *>(w + space.mid);
     const int64_t chunk = (rows + chunks - 1) / chunks;
-    hipLaunchKernelGGL((norm_column_kernel<T>), dim3(cols, chunks), dim3(1024), 0, st, part, mid, dg, db, rows, chunk, c);
-    hipLaunchKernelGGL((norm_column_kernel<T>), dim3(cols), dim3(1024), 0, st, mid, nullptr, dg, db,
+    hipLaunchKernelGGL((norm_column_kernel<T>), dim3(cols, chunks), dim3(kColumnThreads), 0, st, part, mid, dg, db, rows, chunk, c);
+    hipLaunchKernelGGL((norm_column_kernel<T>), dim3(cols), dim3(kColumnThreads), 0, st, mid, nullptr, dg, db,
                        static_cast<int64_t>(chunks), static_cast<int64_t>(chunks), c);
     return done();
 }
@@ -1273,6 +1276,7 @@ int64_t norm_workspace(int pass, const NormSizes &s) {
 // where its launch does; the join's own launch, of at most 64 lanes a group, is of at most 1024 / 3 spans of at most
 // kSpan groups (three slabs or more, see map_grid()).
 bool norm_grid_ok(int pass, const NormSizes &s) {
+    if (pass == 1 && int64_t{column_blocks(s.c)} * kColumnThreads > UINT32_MAX) return false;
     if (token_form(s)) return token_grid(s, pass).gblocks <= 65535;
     if (!two_pass(s, pass)) return true;
     const MapGrid m = map_grid(s);

@@ -56,3 +56,14 @@ def test_the_checkpoints_limit():
     import dynamic_convolution_amd._sequence as S
     assert S._lib().act8_pack(F, F + STEP, F + 2 * STEP, (1 << 32) - 255, 32, 0, None) == TOO_LARGE
     assert S._lib().act8_pack(F, F, F, (1 << 32) - 256, 32, 0, None) == -7  # overlapping: past the limits' check
+
+
+def test_column_sums_launch():
+    """32 of the 2 c columns of the gradients' sums go to 1024 threads: 2^32 of them at c = 2^26, which the forward serves."""
+    for c, groups, fits in (((1 << 26) - 2048, (1 << 15) - 1, True), (1 << 26, 1 << 15, False)):
+        dc.groupnorm_act_workspace_bytes(0, 1, 1, c, groups, torch.float16)
+        if fits:
+            dc.groupnorm_act_workspace_bytes(1, 1, 1, c, groups, torch.float16)
+        else:
+            with pytest.raises(dc.DwconvError, match="DW_ETOOLARGE"):
+                dc.groupnorm_act_workspace_bytes(1, 1, 1, c, groups, torch.float16)
