@@ -5,13 +5,13 @@
 //
 // The checks themselves are in _sequence.py: it makes a plan once for each key and keeps it.  Nothing here is kept from call to
 // call.
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
 
 #include <cstdint>
 #include <cstring>
-#include <exception>
 #include <vector>
 
 #include "dwseq.h"
@@ -26,14 +26,11 @@ const at::Tensor *tensor(PyObject *o) {
     return &THPVariable_Unpack(o);
 }
 
-// C++ exceptions end here as Python ones.
+// C++ exceptions end here as the Python ones that torch makes of them: no memory for an output is its OutOfMemoryError.
 template <typename F> PyObject *guarded(F f) {
-    try {
-        return f();
-    } catch (const std::exception &e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
-    }
+    HANDLE_TH_ERRORS
+    return f();
+    END_HANDLE_TH_ERRORS
 }
 
 // key(*tensors or None) -> bytes: shapes, strides, types and devices.
