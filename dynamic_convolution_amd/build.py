@@ -11,6 +11,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import shutil
 import subprocess
 import sys
 
@@ -72,9 +73,9 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError("link failed:\n%s" % r.stdout)
     os.replace(tmp, LIB)
     build_probe()
-    build_bind()
+    bind = build_bind()
     if verbose:
-        print("built", LIB, PROBE_LIB, "and", BIND_LIB)
+        print("built", LIB, PROBE_LIB, "and", bind or "%s left out: it needs torch" % os.path.basename(BIND_LIB))
     return LIB
 
 
@@ -89,25 +90,30 @@ def build_probe() -> str:
     return PROBE_LIB
 
 
-def build_bind() -> str:
-    """Compile the sequence operators' binding into _seqbind.so, which loads libdwconv.so beside it."""
+def build_bind():
+    """Compile the sequence operators' binding into _seqbind.so, which loads libdwconv.so beside it; returns its path, or
+    None where there is no torch: the library does without, and the binding takes torch's tensors."""
     import sysconfig
 
-    import torch
-    from torch.utils.cpp_extension import include_paths, library_paths
+    try:
+        import torch
+        from torch.utils.cpp_extension import include_paths, library_paths
+    except ImportError:
+        return None
     tmp = BIND_LIB + ".tmp%d" % os.getpid()
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+    cxx = os.environ.get("CXX") or ("g++" if shutil.which("g++") else HIPCC)
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I" + INCLUDE,
            "-isystem", sysconfig.get_path("include")]
     for path in include_paths():
         cmd += ["-isystem", path]
-    cmd += [BIND_SRC, "-o", tmp]
+    cmd += ["-x", "c++", BIND_SRC, "-x", "none", "-o", tmp]  # hipcc would take it for HIP code
     for path in library_paths():
         cmd += ["-L" + path]
     cmd += ["-ltorch_python", "-ltorch_cpu", "-lc10", "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     if r.returncode != 0:
-        raise RuntimeError("g++ failed for %s:\n%s" % (BIND_SRC, r.stdout))
+        raise RuntimeError("%s failed for %s:\n%s" % (cxx, BIND_SRC, r.stdout))
     os.replace(tmp, BIND_LIB)
     return BIND_LIB
 
