@@ -409,8 +409,8 @@ __device__ __forceinline__ void add_chunk(int lane, f32x4 (&z)[DKP / 16], const 
 }
 
 template <typename T, int DKP>
-__global__ __launch_bounds__(kWG, (Tile<T, DKP>::waves)) void decay_state_kernel(AttnLaunch l, float *seg0, float *seg1,
-                                                                                   float *seg2) {
+__global__ __launch_bounds__(kWG, (Tile<T, DKP>::waves)) void decay_state_kernel(AttnLaunch l, float *seg0,
+                                                                                   float *seg1) {
     using L = Tile<T, DKP>;
     __shared__ __align__(16) uint16_t kt[L::NP * L::C * L::KS];
     __shared__ __align__(16) uint16_t vt[L::NP * L::C * L::VS];
@@ -457,7 +457,7 @@ __global__ __launch_bounds__(kWG, (Tile<T, DKP>::waves)) void decay_state_kernel
         }
         __syncthreads();
     }
-    float *seg = ri == 0 ? seg0 : ri == 1 ? seg1 : seg2;
+    float *seg = ri == 0 ? seg0 : seg1;
     seg += (static_cast<int64_t>(w.pair) * l.nseg + w.seg) * r.dk * r.dv;
     store_state<DKP>(seg, z, w.vb * kVB + 16 * wave + (threadIdx.x & 15), r.dk, r.dv);
 }
@@ -961,11 +961,11 @@ int attn_out_launch(const AttnLaunch &l, int dtype, hipStream_t stream) {
     });
 }
 
-int attn_state_launch(const AttnLaunch &l, float *const seg[3], int dtype, hipStream_t stream) {
+int attn_state_launch(const AttnLaunch &l, float *const seg[2], int dtype, hipStream_t stream) {
     return by_type(dtype, [&](auto tag) {
         return by_size(l.dkp, [&](auto d) {
             hipLaunchKernelGGL((decay_state_kernel<decltype(tag), decltype(d)::value>), dim3(blocks_of(l)), dim3(kWG),
-                               0, stream, l, seg[0], seg[1], seg[2]);
+                               0, stream, l, seg[0], seg[1]);
             return done();
         });
     });

@@ -60,8 +60,8 @@ struct AttnLaunch {
 // Kernels' launchers: kOk, kErrHip or kErrUnsupported (dw_internal.hpp).
 AttnPlan attn_plan(const AttnSizes &s, int nroles);
 int attn_out_launch(const AttnLaunch &l, int dtype, hipStream_t stream);
-// Every segment's own state from zero into seg (pair, segment, dk, dv); q of the roles is not read.
-int attn_state_launch(const AttnLaunch &l, float *const seg[3], int dtype, hipStream_t stream);
+// Every segment's own state from zero into the role's seg (pair, segment, dk, dv); q of the one or two roles is not read.
+int attn_state_launch(const AttnLaunch &l, float *const seg[2], int dtype, hipStream_t stream);
 // Turns the segments' own states (pair, segment, dk, dv) into the states before each segment.
 struct AttnScan {
     float *seg;

@@ -273,7 +273,7 @@ int decayattn_fwd(const void *q, const void *k, const void *v, const float *log_
     else set_state(&r, state, size, 0, false), r.zout = state_out;
     add_role(&l, r);
     if (plan.nseg > 1) {
-        float *const segs[3] = {seg, nullptr, nullptr};
+        float *const segs[2] = {seg, nullptr};
         rc = dw::attn_state_launch(l, segs, dtype, st);
         if (rc == dw::kOk)
             rc = dw::attn_scan_launch({seg, state, state_out}, {}, log_decay, lengths, l.b, l.h, t, s.dk, s.dv, plan.nseg,
@@ -331,8 +331,7 @@ int decayattn_bwd(const void *q, const void *k, const void *v, const float *log_
     const float *z[2] = {state, dstate_out};
     int64_t pair = size, step = 0;
     if (plan.nseg > 1) {
-        float *const seg[3] = {reinterpret_cast<float *>(ws + space.seg[0]), reinterpret_cast<float *>(ws + space.seg[1]),
-                               nullptr};
+        float *const seg[2] = {reinterpret_cast<float *>(ws + space.seg[0]), reinterpret_cast<float *>(ws + space.seg[1])};
         dw::AttnLaunch l = launch_of(s, plan, log_decay, lengths);
         dw::AttnRole r = role_of(pq, pk, pv);
         r.s_upd = 1.f;
