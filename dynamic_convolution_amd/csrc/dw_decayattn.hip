@@ -906,10 +906,10 @@ uint32_t blocks_of(const AttnLaunch &l) {
 // keys and values are read twice, the segments' states go to memory and back, and two or three small
 // launches are added.  The fewest microseconds of a simple account are taken: a chunk costs a workgroup
 // u when it has its CU to itself, 2 u with another beside it; half of that for the segments'
-// own states; four passes over those at 5 TB/s.  u is 4 for 64 tokens of 128 x 128 bf16 heads.  (8
-// sequences of 4096 tokens, 8 heads, gradients: 2 segments 296 us, 3 298, 4 269, 6 288, 8 283; 2 sequences of
-// 16384, 8 heads: 11 segments 151 us, 16 123, 22 137, 32 130, 64 147; gradients of 2 of 301, 4 heads, fp32: 3
-// segments 39 us, 5 29, 10 25.)
+// own states; four passes over those at 5 TB/s.  u is 4 for 64 tokens of 128 x 128 bf16 heads.  (Gradients of 8
+// sequences of 4096 tokens, 8 heads: 1 segment 243 us, 2 290, 3 298, 4 267, 6 289, 8 282; 2 sequences of
+// 16384, 8 heads: 8 segments 192 us, 11 155, 16 126, 22 139, 32 129, 64 150; gradients of 2 of 301, 4 heads, fp32: 1
+// segment 48 us, 3 39, 5 29, 10 25.  The account takes 1, 16 and 10.)
 AttnPlan attn_plan(const AttnSizes &s, int nroles) {
     const int dkp = padded(nroles > 1 ? std::max(s.dk, s.dv) : s.dk);
     AttnPlan p;
