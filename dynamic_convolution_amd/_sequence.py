@@ -269,6 +269,7 @@ def decayattn_fwd(q, k, v, log_decay, scale=None, state=None, lengths=None, out=
     (float32).  scale: dk ** -0.5 if None.  state (b, h, dk, dv) float32: before the first token,
     zeros if None.  lengths (b) int32: tokens of each sequence, the rest is padding, whose output
     is zero.  Returns o (b, t, h, dv) and the float32 state after each sequence's last token.
+    A value that is not finite spreads over its 64-token chunk, to the tokens before it too, and after it.
     """
     B = _bind or _binding()
     key = B.key(q, k, v, log_decay, state, lengths)

@@ -55,7 +55,7 @@ typedef __attribute__((address_space(1))) char global_char;
 // A workgroup has eight waves, 16 value columns each; two workgroups fit a CU.  With four waves of 32
 // columns (half the LDS reads) the matrix and vector pipes were idle half of the time.  What bounds the output pass is
 // vector and matrix issue: a chunk of 64 tokens of 128 x 128 bf16 heads is 460 and 81 instructions a wave, 3.8 us for
-// a workgroup alone on its CU and twice that for two (gradients of 8 x 4096 tokens, 8 heads: 240 us).
+// a workgroup alone on its CU and twice that for two (gradients of 8 x 4096 tokens, 8 heads: 242 us).
 constexpr int kWG = 512;
 constexpr int kVB = 128;  // value columns of a workgroup
 
