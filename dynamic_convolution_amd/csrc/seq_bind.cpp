@@ -23,7 +23,12 @@ const at::Tensor *tensor(PyObject *o) {
         PyErr_Format(PyExc_TypeError, "expected a tensor, not %s", Py_TYPE(o)->tp_name);
         return nullptr;
     }
-    return &THPVariable_Unpack(o);
+    const at::Tensor &t = THPVariable_Unpack(o);
+    if (t.is_neg()) {  // its memory holds the values before torch negates them
+        PyErr_SetString(PyExc_TypeError, "a tensor is negated lazily; call its resolve_neg()");
+        return nullptr;
+    }
+    return &t;
 }
 
 // C++ exceptions end here as the Python ones that torch makes of them: no memory for an output is its OutOfMemoryError.

@@ -51,3 +51,14 @@ def test_inference_tensors_have_no_version():
     call("attn_step", tensors, CALLS[2][3])
     with torch.inference_mode():
         call("attn_step", tensors, CALLS[2][3])
+
+
+def test_tensors_that_are_negated_later_are_refused():
+    """Such a view's memory holds the values before torch negates them."""
+    x = torch.ones((2, 3))
+    with pytest.raises(TypeError, match="resolve_neg"):
+        S._binding().key(torch._neg_view(x))
+    name, _, _, numbers = CALLS[4]
+    with pytest.raises(TypeError, match="resolve_neg"):
+        call(name, [torch.zeros(8), torch.zeros(8), torch._neg_view(torch.zeros(8))], numbers)
+    assert S._binding().key(torch._neg_view(x).resolve_neg()) == S._binding().key(x)
